@@ -31,19 +31,19 @@
 // A padded batch of up to 32 sequences is dealt to the clusters by the kernel itself (deal_tiles): every
 // CTA reads the lengths, and the sequences with the most tiles split theirs over a cluster while the
 // others' row tiles take a CTA each, by the threshold that ends first.  3 canvases of 500 over 4500 keys,
-// 72 to 80 row tiles in use: split all or none, 68 and 53 us; dealt 49 us (47.4 by now).
+// 72 to 80 row tiles in use: split all or none, 68 and 53 us; dealt 49 us (51.3 by now, with weights from 2^5).
 //
 // What bounds it: the chain of a unit, not the pipe.  hd 256, 16-bit: a tile's products take 1024 clocks,
 // its softmax 960 (the wait for the scores 240, their load and maximum 310, exponentials 360, stores 60)
-// and, in about a third of the tiles, O's move to another reference 780: 1450 a tile together; 4-bit
-// tiles, whose unpacking shares the issue slots, 1850.  Two threads a row halve neither (the exchange of
+// and, in about two tiles of five, O's move to another reference 780: 1600 a tile together; 4-bit
+// tiles, whose unpacking shares the issue slots, 2000.  Two threads a row halve neither (the exchange of
 // their maxima costs what they save), and registers in place of the ring for 4-bit codes change nothing.
 // hd 128: the products of two CTAs an SM (640 clocks a tile each, since Q comes from shared memory) hold
 // their loops at 1360 clocks a tile; a CTA's start and end, 14 k clocks of 38 k, leave the pipe to the other
 // one alone; and there are four rounds of CTAs where 3.4 are full.
 // Measured: 8192 tokens of 16 heads of 128, window 1024: 77.5 us (0.83 PFLOP/s); 3 canvases of 500 over
-// 4500 keys at hd 256: 47.4 us; 512 over 8704 4-bit keys at hd 256: 48.3 us (0.76 PFLOP/s), of which the
-// start takes 13 k clocks of 88 k and the merge 14 k.
+// 4500 keys at hd 256: 51.3 us; 512 over 8704 4-bit keys at hd 256: 51.4 us (0.71 PFLOP/s), of which the
+// start takes 13 k clocks of 95 k and the merge 14 k.
 #pragma once
 #include "sm103_ptx.cuh"
 #include "window_rows.cuh"
@@ -104,12 +104,15 @@ template <int HD, int KIND> struct TileCfg {
     static_assert(SOFT_REGS * NQT + (Q4 ? 2 * CONV_REGS : 0) + REST_REGS <= REGS * (THREADS / 128), "register pool");
 };
 
-// A row's reference is set kHeadroom above its largest score (log2 units), so weights start at
-// 2^-kHeadroom, and it stays until a score passes it by tile_slack().  f16 weights reach 2^15; a small
-// one is off by 2^-25, 2^-19 of the row's largest weight.  With scores as wide as scale 1 gives (tens
-// of log2 units) most rows then move their reference once at most, where without headroom every second
-// tile of 64 keys had a row in 32 that did, at ~900 clocks.  bf16 has exponents to spare.
-constexpr float kHeadroom = 6.0f;
+// A row's reference is set so that its largest weight so far is 2^tile_lift(), and stays until a weight
+// would pass 2^tile_slack().  f16 weights, over f16 or 4-bit V, reach from 2^15 down to steps of 2^-24: with
+// the largest at 2^-6, keys 13 nats under a leading one (a sink token's lead) weighed nothing, and 8192 of
+// those were half of a result.  From 2^5 on a small weight is off by 2^-30 of the largest, as in the
+// few-row kernel.  The price: O moves in more tiles where scores spread by tens of log2 units (scale 1 at
+// hd 256, partitions of 34 tiles: in 14 of them, 5 with the largest at 2^-6; simulated).  us with lifts of
+// -6, 0, 3, 5 and 8: 3 f16 canvases 47.6, 49.6, 51.2, 51.3, 52.6, the 4-bit one 48, 50.4, 51.2, 51.4, 53.2.
+// bf16 weights have exponents to spare on both sides.
+template <int KIND> constexpr float tile_lift() { return KIND == kTileBf16 ? -6.0f : 5.0f; }
 template <int KIND> constexpr float tile_slack() { return KIND == kTileBf16 ? 60.0f : 15.0f; }
 
 __device__ __forceinline__ void fence_async_shared()
@@ -664,7 +667,7 @@ window_tiles_kernel(const __grid_constant__ WindowMaps maps, const __grid_consta
             best = fmaxf(best, top);
             if (__any_sync(0xffffffffu, top > m + tile_slack<KIND>())) {
                 // every row of the warp moves to its largest score so far: scaling O costs the warp the same
-                const float m_new = fmaxf(m, best + kHeadroom);
+                const float m_new = fmaxf(m, best - tile_lift<KIND>());
                 keep = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
                 l2 = mul_f32x2(l2, make_float2(keep, keep));
                 m = m_new;
