@@ -347,7 +347,7 @@ window_tiles_kernel(const __grid_constant__ WindowMaps maps, const __grid_consta
         for (int i = 0; i < NQT; ++i) mbar_init(&q_ready[i], 4);
         mbar_init(drain, 1);
         fence_mbar_init();
-        if (!Q4) { prefetch_tmap(&maps.k); prefetch_tmap(&maps.v); }
+        if (!Q4 && n > 0) { prefetch_tmap(&maps.k); prefetch_tmap(&maps.v); }      // S = 0: there are none
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, C::TMEM);
