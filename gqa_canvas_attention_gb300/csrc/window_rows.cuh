@@ -2,7 +2,7 @@
 // right form of the operator.
 //
 // out = sum_j e^(z_j - m) v_j / sum_j e^(z_j - m), z_j = scale q.k_j, m the running maximum; sums in
-// fp32.  A row that sees no key is 0.
+// fp32.  A row that sees no key, or only keys of score -inf, is 0.
 #pragma once
 #include "serving.cuh"
 
@@ -75,7 +75,7 @@ __device__ __noinline__ void attend_row(const WindowParams &p, int b, int t, int
 #pragma unroll
         for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
         z *= p.scale;
-        // a score of -inf has weight 0 (a row of nothing else ends as 0 / 0, as in the definition)
+        // a score of -inf has weight 0
         const float top = fmaxf(m, z), keep = l == 0.f ? 0.f : expf(m - top);
         const float w = z == -INFINITY ? 0.f : expf(z - top);
         m = top;
@@ -84,12 +84,14 @@ __device__ __noinline__ void attend_row(const WindowParams &p, int b, int t, int
 #pragma unroll
         for (int i = 0; i < N; ++i) o[i] = fmaf(w, x[i], o[i] * keep);
     }
-    const float inv = sink + see.hi - see.lo > 0 ? 1.0f / l : 0.f;
+    const bool none = l == 0.f;                      // no key has a weight (l is 1 at the least after one that has)
+    const float inv = 1.0f / l;
     const long long oa = b * p.out.batch + t * p.out.token + h * p.out.head + lane * N;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        if (p.bf16) static_cast<__nv_bfloat16 *>(p.out.data)[oa + i] = __float2bfloat16_rn(o[i] * inv);
-        else static_cast<__half *>(p.out.data)[oa + i] = __float2half_rn(o[i] * inv);
+        const float y = none ? 0.f : o[i] * inv;
+        if (p.bf16) static_cast<__nv_bfloat16 *>(p.out.data)[oa + i] = __float2bfloat16_rn(y);
+        else static_cast<__half *>(p.out.data)[oa + i] = __float2half_rn(y);
     }
 }
 

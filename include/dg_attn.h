@@ -390,7 +390,7 @@ int dg_attn_kv4_append(const dg_attn_kv4 *cache, const dg_attn_kv4_args *args, c
  * query i stands at p = kv_len - q_len + i and sees key j iff j < kv_len, j <= p + right
  * (right >= 0; -1: no limit), and j >= p - left (left >= 0; -1: no limit) or j < sinks, the first
  * tokens that stay visible.  out = sum_j softmax_j(scale q.k_j) v_j over the keys it sees; a row that
- * sees none is 0; rows i >= q_len[b] of out are left as they were.  What stands in rows that a query
+ * sees none, or only keys whose scores are -inf, is 0; rows i >= q_len[b] of out are left as they were.  What stands in rows that a query
  * does not see, NaN and infinities included, has no part in it.  kv head of q head h: h / (nh/nkv). */
 typedef struct dg_attn_window_plan dg_attn_window_plan;
 
