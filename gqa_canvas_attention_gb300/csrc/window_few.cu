@@ -728,7 +728,9 @@ window_few_kernel(const __grid_constant__ WindowParams p)
         x.x *= inv; x.y *= inv; x.z *= inv; x.w *= inv;
         if (!any) x = make_float4(0.f, 0.f, 0.f, 0.f);
         const float all = x.x + x.y + x.z + x.w;
-        if (any && !(fabsf(all) <= 3.402823466e38f)) mend[r] = 1;
+        // (but 4-bit, where the row sees every key that was read: its NaN is its own)
+        const bool own = Q4 && sum != 0.f && v.lo == lo && v.hi == hi;
+        if (any && !own && !(fabsf(all) <= 3.402823466e38f)) mend[r] = 1;
         uint2 u;
         if (p.bf16) {
             const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), d = __floats2bfloat162_rn(x.z, x.w);

@@ -28,29 +28,54 @@ __device__ __forceinline__ float half_value(const void *p, long long i, bool bf1
                 : __half2float(static_cast<const __half *>(p)[i]);
 }
 
-// Elements lane * N .. + N - 1 of one key's K (side 0) or V (side 1) row.
-template <int HD, bool KV4>
-__device__ __forceinline__ void key_row(const WindowParams &p, int side, int b, int g, int j, int lane, float *x)
-{
-    constexpr int N = HD / 32;
-    if constexpr (KV4) {
-        const long long cell = ((long long)b * p.nkv + g) * p.S + j;
-        const unsigned char *codes = (side ? p.kv4.v : p.kv4.k) + cell * (HD / 2);
-        const float s = e4m3_value((side ? p.kv4.v_scale : p.kv4.k_scale)[cell * (HD / 16) + lane * N / 16]);
+// A lane's elements lane * N .. + N - 1 of one key's K (side 0) or V (side 1) row, as they lie: N 16-bit
+// values, or N codes and the byte of their scale.
+template <int HD, bool KV4> struct KeyPart {
+    static constexpr int N = HD / 32, BYTES = KV4 ? N / 2 : 2 * N;
+    uint32_t w[BYTES < 4 ? 1 : BYTES / 4];
+    unsigned char scale;
+
+    __device__ __forceinline__ void load(const WindowParams &p, int side, int b, int g, int j, int lane)
+    {
+        if constexpr (KV4) {
+            const long long cell = ((long long)b * p.nkv + g) * p.S + j;
+            const unsigned char *at = (side ? p.kv4.v : p.kv4.k) + cell * (HD / 2) + lane * BYTES;
+            scale = (side ? p.kv4.v_scale : p.kv4.k_scale)[cell * (HD / 16) + lane * N / 16];
+            if constexpr (BYTES == 1) w[0] = *at;
+            else if constexpr (BYTES == 2) w[0] = *reinterpret_cast<const unsigned short *>(at);
+            else w[0] = *reinterpret_cast<const uint32_t *>(at);
+        } else {
+            const Rows &r = side ? p.v : p.k;
+            const char *at = static_cast<const char *>(r.data) + 2 * (b * r.batch + j * r.token + g * r.head) + lane * BYTES;
+            if constexpr (BYTES == 4) w[0] = *reinterpret_cast<const uint32_t *>(at);
+            else if constexpr (BYTES == 8) {
+                const uint2 x = *reinterpret_cast<const uint2 *>(at);
+                w[0] = x.x; w[1] = x.y;
+            } else {
+                const uint4 x = *reinterpret_cast<const uint4 *>(at);
+                w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void widen(float *x, bool bf16) const
+    {
+        const float s = KV4 ? e4m3_value(scale) : 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int e = lane * N + i;
-            x[i] = e2m1_value(codes[e / 2] >> (4 * (e & 1))) * s;
+            if constexpr (KV4) {
+                x[i] = e2m1_value(w[0] >> (4 * i)) * s;
+            } else {
+                const unsigned short h = (unsigned short)(w[i / 2] >> (16 * (i & 1)));
+                x[i] = bf16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
+            }
         }
-    } else {
-        const Rows &r = side ? p.v : p.k;
-        const long long at = b * r.batch + j * r.token + g * r.head + lane * N;
-#pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = half_value(r.data, at + i, p.bf16);
     }
-}
+};
 
-// The whole warp computes row (b, t, h) into out.
+// The whole warp computes row (b, t, h) into out.  The faster kernels call it for rows that end as NaN, up to
+// every row of a call where K or V holds one: 500 rows of 8 heads over 4500 keys of 256 take 27 ms with a NaN
+// in V (one key at a time, an element a load: 90), 0.17 with one in K, which ends a row at once.
+constexpr int kAtOnce = 8;
 template <int HD, bool KV4>
 __device__ __noinline__ void attend_row(const WindowParams &p, int b, int t, int h, int nq, int nk)
 {
@@ -66,23 +91,49 @@ __device__ __noinline__ void attend_row(const WindowParams &p, int b, int t, int
         o[i] = 0.f;
     }
     const int sink = min(p.sinks, see.lo);           // sink keys below the window
-    for (int step = 0; step < sink + see.hi - see.lo; ++step) {
-        const int j = step < sink ? step : see.lo + step - sink;
-        float x[N], z = 0.f;
-        key_row<HD, KV4>(p, 0, b, g, j, lane, x);
+    const int n = sink + see.hi - see.lo;
+    // kAtOnce keys under way at once: a step is the latency of their loads and of 5 shuffles
+    for (int step = 0; step < n; step += kAtOnce) {
+        KeyPart<HD, KV4> k[kAtOnce], v[kAtOnce];
+        float x[N], w[kAtOnce], top = m;
 #pragma unroll
-        for (int i = 0; i < N; ++i) z = fmaf(q[i], x[i], z);
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int i = min(step + u, n - 1), j = i < sink ? i : see.lo + i - sink;
+            k[u].load(p, 0, b, g, j, lane);
+            v[u].load(p, 1, b, g, j, lane);
+        }
 #pragma unroll
-        for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-        z *= p.scale;
-        // a score of -inf has weight 0
-        const float top = fmaxf(m, z), keep = l == 0.f ? 0.f : expf(m - top);
-        const float w = z == -INFINITY ? 0.f : expf(z - top);
+        for (int u = 0; u < kAtOnce; ++u) {
+            k[u].widen(x, p.bf16);
+            w[u] = 0.f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[u] = fmaf(q[i], x[i], w[u]);
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1)
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) w[u] += __shfl_xor_sync(0xffffffffu, w[u], d);
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            w[u] = step + u < n ? w[u] * p.scale : -INFINITY;
+            top = fmaxf(top, w[u]);
+        }
+        const float keep = l == 0.f ? 0.f : expf(m - top);
         m = top;
-        l = l * keep + w;
-        key_row<HD, KV4>(p, 1, b, g, j, lane, x);
+        l *= keep;
 #pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = fmaf(w, x[i], o[i] * keep);
+        for (int i = 0; i < N; ++i) o[i] *= keep;
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            w[u] = w[u] == -INFINITY ? 0.f : expf(w[u] - top);      // a score of -inf has weight 0
+            l += w[u];
+            if (step + u < n) {
+                v[u].widen(x, p.bf16);
+#pragma unroll
+                for (int i = 0; i < N; ++i) o[i] = fmaf(w[u], x[i], o[i]);
+            }
+        }
+        if (l != l) break;                           // NaN, whatever follows
     }
     const bool none = l == 0.f;                      // no key has a weight (l is 1 at the least after one that has)
     const float inv = 1.0f / l;

@@ -49,3 +49,59 @@ def test_scores_of_minus_infinity(T, S, hd, dt):
     out = plan.attend(q, k, v, scale=hd ** -0.5)
     assert not out[:, :, :2].any() and torch.isfinite(out).all()
     assert plan.sync_status() == B.DG_OK
+
+
+def stored(plan_args, seed, dt):
+    """A 4-bit cache of random rows, and its values."""
+    Bn, S, nkv, hd = plan_args
+    cache = B.Kv4Cache(Bn, nkv, S, hd)
+    x = torch.randn(2, Bn, S, nkv, hd, generator=gen(seed), device="cuda").to(TYPES[dt])
+    k, v = torch.zeros_like(x[0]), torch.zeros_like(x[1])
+    cache.append(x[0], x[1], torch.zeros(Bn, dtype=torch.int32, device="cuda"), k_out=k, v_out=v)
+    return cache, k, v
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("T,S,hd", [(1, 700, 128), (5, 3000, 64), (140, 400, 64), (140, 400, 256), (140, 3000, 128),
+                                    (140, 3000, 256)])
+def test_not_a_number_in_the_cache(T, S, hd, dt):
+    """A block of 16 channels that reads as NaN is in the results of the rows that see it, and in no other."""
+    nh, nkv = 4, 2
+    cache, k, v = stored((1, S, nkv, hd), T, dt)
+    q = torch.randn(1, T, nh, hd, generator=gen(S), device="cuda").to(TYPES[dt])
+    plan = B.WindowPlan(nh, nkv, hd, 1, T, S)
+    far = S - T // 2 - 1
+    cache.v_scale[0, 0, far, 1], v[0, far, 0, 16:32] = 0x7F, float("nan")
+    cache.k_scale[0, 1, 3, 0], k[0, 3, 1, :16] = 0x7F, float("nan")
+    for left, right, sinks in ((-1, -1, 0), (-1, 0, 0), (30, 0, 2), (30, 0, 6), (30, 4, 0)):
+        out = plan.attend_kv4(q, cache, left=left, right=right, sinks=sinks, scale=hd ** -0.5)
+        want, tol = plain_attention(q, k, v, None, None, left, right, sinks, hd ** -0.5, torch.zeros_like(out))
+        rows = torch.isnan(want).all(-1)                     # a NaN score: the whole row
+        some = torch.isnan(want).any(-1) & ~rows
+        assert torch.isnan(out[rows]).all() and torch.isnan(out[some][:, 16:32]).all()
+        check_attention(out, want, tol, f"left {left} right {right} sinks {sinks}")
+    assert plan.sync_status() == B.DG_OK
+
+
+@pytest.mark.parametrize("kv4", [False, True], ids=["16bit", "4bit"])
+def test_not_a_number_costs_little(kv4):
+    """A NaN score in every row (and for 4-bit keys a NaN value that every row sees) does not make a call of
+    50 us one of 100 ms: the rows' second computation ends at the first NaN, or is not begun."""
+    nh, nkv, hd, T, S = 8, 4, 256, 512, 8704
+    q = torch.randn(1, T, nh, hd, generator=gen(1), device="cuda").half()
+    plan = B.WindowPlan(nh, nkv, hd, 1, T, S)
+    cache, k, v = stored((1, S, nkv, hd), 2, "f16")
+    for side in ("k", "v") if kv4 else ("k",):
+        if kv4:
+            (cache.k_scale if side == "k" else cache.v_scale)[0, :, 5, 0] = 0x7F
+            call = lambda: plan.attend_kv4(q, cache, scale=hd ** -0.5)
+        else:
+            k[0, 5, :, 0] = float("nan")
+            call = lambda: plan.attend(q, k, v, scale=hd ** -0.5)
+        assert torch.isnan(call()).any(-1).all()
+        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        start.record()
+        call()
+        end.record()
+        torch.cuda.synchronize()
+        assert start.elapsed_time(end) < 10
