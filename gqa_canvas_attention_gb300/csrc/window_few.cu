@@ -339,6 +339,7 @@ window_few_kernel(const __grid_constant__ WindowParams p)
     constexpr int V_AT = TK * P::ROW, KS_AT = 2 * TK * P::ROW, VS_AT = KS_AT + TK * P::SROW;
     constexpr int UPR = P::ROW / 16, CP = TK * UPR / 32;      // 16-byte units of a row, copies of a lane
     auto issue4 = [&](int tile, int stage) {
+        __syncwarp();                                 // every lane has read what stood there
         if (tile >= tile0 && tile < tile1) {
             const int left = tile_left(tile);
             const long long k0 = tile_key(tile);
