@@ -7,7 +7,7 @@
 // x = x (mean x^2 + eps)^-1/2 w first (v: no weight, no rotation), all in fp32 and rounded once.
 //
 // The angle: f_i / 2 pi is held as a 64-bit fraction of a turn, so p * f_i modulo one turn is one
-// wrapping 64-bit integer product, off by at most |p| 2^-65 turns for any position; its upper 32
+// wrapping 64-bit integer product, off by less than |p| 2^-64 turns (of the double f_i); its upper 32
 // bits give the argument of sincospi.  cos and sin are made once a token and shared by its heads.
 //
 // Bound by memory, and next by instruction issue (60 to 65% of the slots): a block takes a few tokens

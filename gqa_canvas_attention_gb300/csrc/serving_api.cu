@@ -350,6 +350,7 @@ dg_attn_rope *dg_attn_rope_create(int hd, int rot_dim, int layout, double theta,
     r->layout = layout;
     r->magnitude = 1.0;
     const double two_pi = 6.283185307179586476925;
+    const double inv_two_pi = 0.15915494309189535, inv_two_pi_rest = -9.839338337591243e-18;    // their sum: to 2^-110
     if (scaling == DG_ROPE_SCALE_NTK) theta *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
     double lo = 0, hi = 0;
     if (scaling == DG_ROPE_SCALE_YARN) {
@@ -367,8 +368,10 @@ dg_attn_rope *dg_attn_rope_create(int hd, int rot_dim, int layout, double theta,
             f = f * (1 - ramp) + f / factor * ramp;
         }
         r->f[i] = f;
-        // f <= 1, so the fraction of a turn is below 1/6 and fits
-        r->turn[i] = (unsigned long long)std::llround(std::ldexp(f / two_pi, 64));
+        // f / 2 pi to 2^-64 of a turn, in two parts (a double alone ends at 2^-56); f <= 1, so it is below 1/6
+        const double turn = f * inv_two_pi, rest = std::fma(f, inv_two_pi, -turn) + f * inv_two_pi_rest;
+        r->turn[i] = (unsigned long long)std::llround(std::ldexp(turn, 64)) +
+                     (unsigned long long)std::llround(std::ldexp(rest, 64));
     }
     return r;
 }

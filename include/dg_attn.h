@@ -349,7 +349,8 @@ typedef struct dg_attn_rope_args {
     float eps;                       /* of the norms */
     dg_attn_rows q, k, v;            /* k may be absent (nkv == 0), v too */
     dg_attn_rows q_out, k_out, v_out;
-    const void *positions;           /* [batch, T], dense; any value, negative ones too */
+    const void *positions;           /* [batch, T], dense; any value, negative ones too: the angle p f_i (f_i as
+                                        dg_attn_rope_frequencies gives it) is off by |p| 2^-64 turns at most */
     const float *q_norm_w, *k_norm_w;/* [hd], 16-byte aligned, or NULL (unweighted) */
 } dg_attn_rope_args;
 

@@ -1,6 +1,9 @@
 """Calls of the serving operators that their declarations allow, at the edges of what they hold.
 
 Plain forms and tolerances are those of test_serving_gpu."""
+import math
+from fractions import Fraction
+
 import pytest
 import torch
 
@@ -105,3 +108,30 @@ def test_not_a_number_costs_little(kv4):
         end.record()
         torch.cuda.synchronize()
         assert start.elapsed_time(end) < 10
+
+
+def pi():
+    """pi to some 60 digits (Machin)."""
+    arctan = lambda n: sum(Fraction((-1) ** i, (2 * i + 1) * n ** (2 * i + 1)) for i in range(60))
+    return 4 * (4 * arctan(5) - arctan(239))
+
+
+@pytest.mark.parametrize("theta,scaling,factor", [(16.0, 0, 1.0), (10000.0, 0, 1.0), (1000000.0, B.DG_ROPE_SCALE_LINEAR, 4.0)])
+def test_angles_of_far_positions(theta, scaling, factor):
+    """cos and sin of p f to fp32, f the frequency that the rope reports, for positions far beyond 32 bits.
+
+    The angle is off by |p| 2^-64 turns and 2^-33 of its rounding to 32 bits, its argument by 2^-25 of a half
+    turn, the results by 2 ulp."""
+    far = [3, 2 ** 31 + 5, -(2 ** 36) - 1, 2 ** 40 + 12345, 2 ** 44 + 7, -(2 ** 44) + 3]
+    rope = B.Rope(64, 8, theta=theta, scaling=scaling, factor=factor)
+    x = torch.zeros(1, len(far), 1, 64, device="cuda")
+    x[..., :4] = 1                                           # pairs (1, 0)
+    y, _ = rope.apply(x, None, torch.tensor([far], device="cuda"))
+    f, _ = rope.frequencies()
+    two_pi = 2 * pi()
+    for n, p in enumerate(far):
+        for i in range(4):
+            angle = float((Fraction(f[i]) * p) % two_pi)
+            tol = 2 * math.pi * (abs(p) * 2.0 ** -64 + 2.0 ** -33 + 2.0 ** -26) + 4 * 2.0 ** -24
+            assert abs(float(y[0, n, 0, i]) - math.cos(angle)) <= tol, (p, i)
+            assert abs(float(y[0, n, 0, 4 + i]) - math.sin(angle)) <= tol, (p, i)
