@@ -189,8 +189,7 @@ window_few_kernel(const __grid_constant__ WindowParams p)
     __shared__ float2 ml[kWarps][ROWS];
     __shared__ int last_here, mend[ROWS];
     __shared__ int seq_tiles[kFewSequences];
-    __shared__ long long scan[4];                     // units before the run's sequence, that sequence, all units,
-                                                      // pairs with some
+    __shared__ long long scan[2];                     // units before the run's sequence, that sequence
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
