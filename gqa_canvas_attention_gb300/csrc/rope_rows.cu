@@ -19,6 +19,8 @@
 // step of single tokens takes 7.7 us, the host's, and 2.1 us in a graph.
 #include "serving.cuh"
 
+#include <atomic>
+
 namespace dg {
 namespace {
 
@@ -234,10 +236,27 @@ __global__ void __launch_bounds__(kThreads, IN_WIDE ? 3 : 5) rope_rows_kernel(co
     }
 }
 
+// SMs of the current device, asked for once a device.
+cudaError_t sm_count(int &n)
+{
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices];
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    n = e == cudaSuccess && device < kDevices ? known[device].load(std::memory_order_relaxed) : 0;
+    if (e != cudaSuccess || n > 0) return e;
+    e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device);
+    if (e == cudaSuccess && device < kDevices) known[device].store(n, std::memory_order_relaxed);
+    return e;
+}
+
 template <int HD>
 cudaError_t launch_hd(RopeRowsParams &p, cudaStream_t s)
 {
     constexpr int NS = kThreads / (HD / 8);
+    int sms = 0;
+    cudaError_t e = sm_count(sms);
+    if (e != cudaSuccess) return e;
     if (p.T == 1) {
         // single tokens: the batch is the run of tokens
         p.T = p.batch;
@@ -255,11 +274,10 @@ cudaError_t launch_hd(RopeRowsParams &p, cudaStream_t s)
     const int groups = (p.H + NS - 1) / NS;
     long long rows = (long long)p.batch * p.T * groups;
     p.tokens_per_block = p.norm || p.interleaved ? kTokens : kTokens / 2;
-    while (p.tokens_per_block > 1 && rows / p.tokens_per_block < 2 * 152) p.tokens_per_block /= 2;
+    while (p.tokens_per_block > 1 && rows / p.tokens_per_block < 2 * sms) p.tokens_per_block /= 2;
     const dim3 grid((p.T + p.tokens_per_block - 1) / p.tokens_per_block, groups, p.batch < 65535 ? p.batch : 65535);
     const bool iw = p.in_type == kRowF32, ow = p.out_type == kRowF32;
     const size_t smem = (size_t)p.tokens_per_block * (p.rot * sizeof(float) + kThreads * (iw ? 32 : 16));
-    cudaError_t e = cudaSuccess;
     auto launch = [&](auto kernel) {
         // beyond 48 KB: fp32 rows of 8 tokens
         if (smem > 49152) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
