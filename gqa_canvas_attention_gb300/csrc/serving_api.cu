@@ -57,14 +57,21 @@ struct Tensor {
     }
 };
 
+// Elements that a dimension reaches over at most, so that byte offsets of three of them stay in 64 bits.
+constexpr long long kMaxExtent = 1LL << 57;
+
 int check_layout(const Tensor &t)
 {
     if (!t.r->data) return fail(DG_ERR_ARG, "%s is NULL", t.name);
     if (!aligned16(t.r->data)) return fail(DG_ERR_ALIGN, "%s is not 16-byte aligned", t.name);
-    for (int d = 0; d < 3; ++d)
-        if (t.n[d] > 1 && (t.stride(d) * t.size) % 16)
+    for (int d = 0; d < 3; ++d) {
+        if (t.n[d] <= 1) continue;
+        if (t.stride(d) > kMaxExtent / t.n[d] || t.stride(d) < -kMaxExtent / t.n[d])
+            return fail(DG_ERR_ARG, "%s: a stride of %lld elements leaves the address space", t.name, t.stride(d));
+        if ((t.stride(d) * t.size) % 16)
             return fail(DG_ERR_ALIGN, "%s: a stride of %lld elements is not a multiple of 16 bytes", t.name,
                         t.stride(d));
+    }
     return DG_OK;
 }
 
@@ -82,22 +89,55 @@ int check_distinct(const Tensor &t)
     return DG_OK;
 }
 
-// Whether two tensors may share bytes: their ranges meet, and they are not two slices of the heads of
-// one buffer (same batch and token pitch, apart within a token).
+// One term of the distance between a row of one tensor and a row of another: step * x, x in [lo, hi].
+struct Term {
+    long long step, lo, hi;
+};
+
+// Whether distance + sum step_i x_i can lie in (-before, after); terms in falling order of their steps, all
+// positive.  Each term leaves few x, since the smaller ones reach less far than one step of it in any usual
+// layout; where that is not so and `budget` runs out, the answer is yes.
+bool can_meet(const Term *t, int n, long long distance, long long before, long long after, int &budget)
+{
+    if (n == 0) return -before < distance && distance < after;
+    long long low = distance, high = distance;       // with the smaller terms at their ends
+    for (int i = 1; i < n; ++i) {
+        low += t[i].step * t[i].lo;
+        high += t[i].step * t[i].hi;
+    }
+    auto floor_div = [](long long a, long long b) { return a / b - (a % b < 0); };
+    const long long from = std::max(t->lo, floor_div(-before - high, t->step) + 1);
+    const long long to = std::min(t->hi, -(floor_div(low - after, t->step) + 1));
+    for (long long x = from; x <= to; ++x) {
+        if (--budget < 0) return true;
+        if (can_meet(t + 1, n - 1, distance + t->step * x, before, after, budget)) return true;
+    }
+    return false;
+}
+
+// Whether two tensors share bytes, as slices of one buffer do not although their ranges meet.
 bool may_overlap(const Tensor &a, const Tensor &b)
 {
     if (a.end() <= b.first() || b.end() <= a.first()) return false;
-    auto pitch = [](const Tensor &t, int d) { return t.stride(d) * t.size; };
-    for (int d = 0; d < 2; ++d)
-        if (a.n[d] != b.n[d] || (a.n[d] > 1 && (pitch(a, d) != pitch(b, d) || pitch(a, d) <= 0))) return true;
-    if (pitch(a, 2) < 0 || pitch(b, 2) < 0) return true;
-    long long step = a.n[1] > 1 ? pitch(a, 1) : a.n[0] > 1 ? pitch(a, 0) : 0;
-    if (!step || (a.n[1] > 1 && a.n[0] > 1 && pitch(a, 0) % step)) return true;
-    const long long wa = (a.n[2] > 1 ? pitch(a, 2) * (a.n[2] - 1) : 0) + (long long)a.hd * a.size;
-    const long long wb = (b.n[2] > 1 ? pitch(b, 2) * (b.n[2] - 1) : 0) + (long long)b.hd * b.size;
-    long long gap = (static_cast<const char *>(b.r->data) - static_cast<const char *>(a.r->data)) % step;
-    if (gap < 0) gap += step;
-    return !(gap >= wa && gap + wb <= step);
+    Term t[6];
+    int n = 0;
+    for (int side = 0; side < 2; ++side) {
+        const Tensor &x = side ? b : a;
+        for (int d = 0; d < 3; ++d) {
+            const long long step = x.stride(d) * x.size * (side ? 1 : -1), last = x.n[d] - 1;
+            if (step == 0 || last == 0) continue;
+            const Term one = {std::llabs(step), step > 0 ? 0 : -last, step > 0 ? last : 0};
+            int i = 0;
+            while (i < n && t[i].step != one.step) ++i;
+            if (i == n) t[n++] = {one.step, 0, 0};
+            t[i].lo += one.lo;
+            t[i].hi += one.hi;
+        }
+    }
+    std::sort(t, t + n, [](const Term &x, const Term &y) { return x.step > y.step; });
+    int budget = 2000;
+    return can_meet(t, n, static_cast<const char *>(b.r->data) - static_cast<const char *>(a.r->data),
+                    (long long)b.hd * b.size, (long long)a.hd * a.size, budget);
 }
 
 bool same_rows(const Tensor &a, const Tensor &b)
@@ -206,7 +246,8 @@ int rope_rows(const dg_attn_rope *rope, const dg_attn_rope_args *a, bool norm, c
 int check_cache(const dg_attn_kv4 *c)
 {
     if (!c) return fail(DG_ERR_ARG, "NULL cache");
-    if (c->batch < 1 || c->nkv < 1 || c->cap < 1 || (c->hd != 64 && c->hd != 128 && c->hd != 256))
+    if (c->batch < 1 || c->nkv < 1 || c->cap < 1 || (c->hd != 64 && c->hd != 128 && c->hd != 256) ||
+        (long long)c->batch * c->nkv > (1LL << 48) / c->cap)
         return fail(DG_ERR_ARG, "cache of batch %d, nkv %d, cap %d, hd %d", c->batch, c->nkv, c->cap, c->hd);
     if (!c->k || !c->k_scale || !c->v || !c->v_scale) return fail(DG_ERR_ARG, "a cache buffer is NULL");
     if (!aligned16(c->k) || !aligned16(c->k_scale) || !aligned16(c->v) || !aligned16(c->v_scale))

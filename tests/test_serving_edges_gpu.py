@@ -135,3 +135,29 @@ def test_angles_of_far_positions(theta, scaling, factor):
             tol = 2 * math.pi * (abs(p) * 2.0 ** -64 + 2.0 ** -33 + 2.0 ** -26) + 4 * 2.0 ** -24
             assert abs(float(y[0, n, 0, i]) - math.cos(angle)) <= tol, (p, i)
             assert abs(float(y[0, n, 0, 4 + i]) - math.sin(angle)) <= tol, (p, i)
+
+
+def test_one_buffer_of_heads_outside_tokens():
+    """q, k and v as slices of one [batch, heads, T, hd] buffer: in place, and from one half into the other."""
+    Bn, T, nh, nkv, hd = 3, 9, 4, 2, 64
+    H = nh + 2 * nkv
+    rope = B.Rope(hd)
+    buf = torch.randn(Bn, H, T, hd, generator=gen(1), device="cuda").bfloat16()
+    keep = buf.clone()
+    pos = torch.arange(T, device="cuda").repeat(Bn, 1)
+    q, k, v = (buf[:, a:b].transpose(1, 2) for a, b in ((0, nh), (nh, nh + nkv), (nh + nkv, H)))
+    q0, k0, v0 = (keep[:, a:b].transpose(1, 2) for a, b in ((0, nh), (nh, nh + nkv), (nh + nkv, H)))
+    want = rope.qk_norm(q0, k0, v0, pos)
+    rope.qk_norm(q, k, v, pos, q_out=q, k_out=k, v_out=v)
+    for x, y in zip((q, k, v), want):
+        assert torch.equal(x, y)
+    rope.apply(k0, None, pos, q_out=q0[:, :, :nkv])
+    assert torch.equal(q0[:, :, :nkv], rope.apply(k0, None, pos)[0])
+    # the attention's output into other heads of its queries' buffer
+    plan = B.WindowPlan(nkv, nkv, hd, Bn, T, T)
+    kk, vv = torch.randn(2, Bn, T, nkv, hd, generator=gen(2), device="cuda").bfloat16()
+    want = plan.attend(q[:, :, :nkv], kk, vv)
+    plan.attend(q[:, :, :nkv], kk, vv, out=q[:, :, nkv:])
+    assert torch.equal(q[:, :, nkv:], want)
+    with pytest.raises(B.DgAttnError, match="overlaps"):
+        plan.attend(q[:, :, :nkv], kk, vv, out=q[:, :, 1:1 + nkv])
