@@ -524,7 +524,7 @@ window_tiles_kernel(const __grid_constant__ WindowMaps maps, const __grid_consta
         const int t = (mine ? row : row1) / p.G;
         const Visible see = visible_keys(p, nq, nk, t);
         // scores enter as s * zs; a negative scale goes into Q
-        float zs = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-30f);
+        float zs = fabsf(p.scale) * 1.4426950408889634f;
 
         // Q into shared memory, or through the V ring's place into TMEM (a thread its row), in short loops: the
         // code of this phase runs once and comes from L2, 32 unrolled loads of it took 13 k clocks.  A warp
@@ -577,7 +577,8 @@ window_tiles_kernel(const __grid_constant__ WindowMaps maps, const __grid_consta
                 if (top > 0.f && top <= 3.402823466e38f) ex = ilogbf(top);
             }
             const float up = exp2f((float)(-ex / 2)), down = exp2f((float)(-ex - -ex / 2));
-            zs = ldexpf(zs, ex);
+            // the smallest normal at the least: a masked score stays -inf, and scale 0 gives finite scores no weight
+            zs = fmaxf(ldexpf(zs, ex), 1.17549435e-38f);
             if constexpr (C::Q_TMEM) {
 #pragma unroll 1
                 for (int v0 = 0; v0 < HD / 8; v0 += 8) {

@@ -161,3 +161,23 @@ def test_one_buffer_of_heads_outside_tokens():
     assert torch.equal(q[:, :, nkv:], want)
     with pytest.raises(B.DgAttnError, match="overlaps"):
         plan.attend(q[:, :, :nkv], kk, vv, out=q[:, :, 1:1 + nkv])
+
+
+@pytest.mark.parametrize("kv4", [False, True], ids=["16bit", "4bit"])
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-36])
+def test_scale_0_of_large_products(scale, hd, kv4):
+    """Whatever the products are, a scale of 0 (or next to it) makes the weights equal."""
+    S, T = 300, 140
+    big = 1e32 if kv4 else 1e16
+    q = (torch.randn(1, T, 4, hd, generator=gen(hd), device="cuda") * big).bfloat16()
+    plan = B.WindowPlan(4, 2, hd, 1, T, S)
+    if kv4:
+        cache, k, v = stored((1, S, 2, hd), 3, "bf16")
+        out = plan.attend_kv4(q, cache, scale=scale)
+    else:
+        k, v = torch.randn(2, 1, S, 2, hd, generator=gen(4), device="cuda").bfloat16()
+        k = (k * big).bfloat16()
+        out = plan.attend(q, k, v, scale=scale)
+    want, tol = plain_attention(q, k, v, None, None, -1, -1, 0, scale, torch.zeros_like(out))
+    check_attention(out, want, tol)
