@@ -728,9 +728,7 @@ window_few_kernel(const __grid_constant__ WindowParams p)
         x.x *= inv; x.y *= inv; x.z *= inv; x.w *= inv;
         if (!any) x = make_float4(0.f, 0.f, 0.f, 0.f);
         const float all = x.x + x.y + x.z + x.w;
-        // (but 4-bit, where the row sees every key that was read: its NaN is its own)
-        const bool own = Q4 && sum != 0.f && v.lo == lo && v.hi == hi;
-        if (any && !own && !(fabsf(all) <= 3.402823466e38f)) mend[r] = 1;
+        if (any && !(fabsf(all) <= 3.402823466e38f)) mend[r] = sum == 0.f ? 2 : 1;
         uint2 u;
         if (p.bf16) {
             const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), d = __floats2bfloat162_rn(x.z, x.w);
@@ -831,7 +829,10 @@ window_few_kernel(const __grid_constant__ WindowParams p)
     }
     __syncthreads();
     for (int r = warp; r < rows; r += kWarps)
-        if (mend[r]) attend_row<HD, Q4>(p, b, r / p.G, gh * p.G + r % p.G, nq, nk);
+        if (mend[r]) {
+            if constexpr (Q4) mend_row_kv4<HD>(p, b, gh, r, nq, nk, 0, rows - 1, mend[r] == 2);
+            else attend_row<HD, Q4>(p, b, r / p.G, gh * p.G + r % p.G, nq, nk);
+        }
     // on to the next pair of the run
     unit += tile1 - tile0;
     if (unit >= unit_end) break;

@@ -146,6 +146,19 @@ __device__ __noinline__ void attend_row(const WindowParams &p, int b, int t, int
     }
 }
 
+// Row `row` (t * G + h mod G) of kv head g over 4-bit keys, which ended as NaN in a kernel that reads every key
+// that the rows first .. last see: once more, if there are keys that it does not see, or if no key has a weight
+// (`empty`).  Its NaN is its own otherwise: a 4-bit V holds no infinity that a weight rounded to 0 would make one.
+template <int HD>
+__device__ __noinline__ void mend_row_kv4(const WindowParams &p, int b, int g, int row, int nq, int nk, int first, int last,
+                                          bool empty)
+{
+    const Visible v = visible_keys(p, nq, nk, row / p.G);
+    if (empty || v.lo != visible_keys(p, nq, nk, first / p.G).lo ||
+        v.hi != visible_keys(p, nq, nk, min(last, nq * p.G - 1) / p.G).hi)
+        attend_row<HD, true>(p, b, row / p.G, g * p.G + row % p.G, nq, nk);
+}
+
 // Lengths of sequence b, held to the buffers.
 __device__ __forceinline__ int query_count(const WindowParams &p, int b)
 {

@@ -740,12 +740,6 @@ window_tiles_kernel(const __grid_constant__ WindowMaps maps, const __grid_consta
         const uint32_t to = tbase + lane_off + C::O_COL + (NQT == 2 ? q * HD : 0);
         uint32_t sent = 0;
         const int b = sequence(), g = kv_head(), parts = partitions();
-        // 4-bit: whether a row sees every key that its block does.  Its NaN is then its own (a 4-bit V holds no
-        // infinity, which a weight that f16 rounds to 0 would make a NaN)
-        auto own_nan = [&](int orow) {
-            const Visible v = visible_keys(p, nq, nk, orow / p.G);
-            return Q4 && v.lo == visible_keys(p, nq, nk, row0 / p.G).lo && v.hi == visible_keys(p, nq, nk, row1 / p.G).hi;
-        };
         if (parts > 1) {
             // CTA k of the cluster owns the rows [k total / parts, (k + 1) total / parts).  Every partition
             // writes its rows into their owners' shared memory (reading them there instead waits a round trip
@@ -828,10 +822,11 @@ window_tiles_kernel(const __grid_constant__ WindowMaps maps, const __grid_consta
                 if (dst) *reinterpret_cast<uint4 *>(dst + 16 * unit) = x;
             }
             __syncwarp();
-            for (unsigned again = __ballot_sync(0xffffffffu, bad && mine && (sum == 0.f || !own_nan(row))); again;
-                 again &= again - 1) {
-                const int orow = row0 + q * 128 + quarter * 32 + (__ffs(again) - 1);
-                attend_row<HD, Q4>(p, b, orow / p.G, g * p.G + orow % p.G, nq, nk);
+            const unsigned empty = Q4 ? __ballot_sync(0xffffffffu, sum == 0.f) : 0;
+            for (unsigned again = __ballot_sync(0xffffffffu, bad && mine); again; again &= again - 1) {
+                const int at = __ffs(again) - 1, orow = row0 + q * 128 + quarter * 32 + at;
+                if constexpr (Q4) mend_row_kv4<HD>(p, b, g, orow, nq, nk, row0, row0 + NQT * 128 - 1, empty >> at & 1);
+                else attend_row<HD, Q4>(p, b, orow / p.G, g * p.G + orow % p.G, nq, nk);
             }
         }
         if (parts > 1) {
@@ -868,7 +863,7 @@ window_tiles_kernel(const __grid_constant__ WindowMaps maps, const __grid_consta
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     if (k < parts) wgt[tid * 8 + k] = any ? mm[k] * inv : 0.f;
-                mend[tid] = any && total_l == 0.f;               // scores of -inf alone
+                mend[tid] = Q4 && any && total_l == 0.f ? 2 : 0;       // scores of -inf alone
                 dst[tid] = static_cast<char *>(p.out.data) + 2 * (b * p.out.batch + ot * p.out.token + oh * p.out.head);
             }
             named_barrier_sync(1, NT);
@@ -894,8 +889,9 @@ window_tiles_kernel(const __grid_constant__ WindowMaps maps, const __grid_consta
                 for (int v = 0; v < U; ++v) {
                     const int i = i0 + v * STEP;
                     if (i >= nr) continue;
-                    if (!(fabsf(x[v].x) + fabsf(x[v].y) + fabsf(x[v].z) + fabsf(x[v].w) <= 3.402823466e38f) && !mend[i])
-                        mend[i] = 2;
+                    if (!(fabsf(x[v].x) + fabsf(x[v].y) + fabsf(x[v].z) + fabsf(x[v].w) <= 3.402823466e38f) &&
+                        (!Q4 || !mend[i]))
+                        mend[i] = 1;
                     *reinterpret_cast<uint2 *>(dst[i] + 2 * ch) =
                         p.bf16 ? make_uint2(pack_bf162(x[v].x, x[v].y), pack_bf162(x[v].z, x[v].w))
                                : make_uint2(pack_half2(x[v].x, x[v].y), pack_half2(x[v].z, x[v].w));
@@ -905,7 +901,8 @@ window_tiles_kernel(const __grid_constant__ WindowMaps maps, const __grid_consta
             for (int i = warp - 4; i < nr; i += 4 * NQT)
                 if (mend[i]) {
                     const int orow = row0 + r0 + i;
-                    if (mend[i] == 1 || !own_nan(orow)) attend_row<HD, Q4>(p, b, orow / p.G, g * p.G + orow % p.G, nq, nk);
+                    if constexpr (Q4) mend_row_kv4<HD>(p, b, g, orow, nq, nk, row0, row0 + NQT * 128 - 1, mend[i] == 2);
+                    else attend_row<HD, Q4>(p, b, orow / p.G, g * p.G + orow % p.G, nq, nk);
                 }
         }
     } else if constexpr (Q4) {
