@@ -461,6 +461,10 @@ class Plan:
 #
 # Tensors of [batch, T, heads, hd] on any strides with a dense last dimension; the C structs they
 # travel in are packed here, field by field as include/dg_attn.h declares them.
+#
+# stream: a torch stream, a raw handle, or None for the current one.  A call on another stream than the
+# one its tensors were allocated on does not tell the allocator so: the caller keeps them alive until the
+# call's work is done (or calls record_stream).
 
 _ROWS = "Pqqq"
 _ROPE_ARGS = struct.Struct("@7if" + 6 * _ROWS + "3P")
@@ -619,6 +623,8 @@ class Rope:
     def apply(self, q, k, positions, q_out=None, k_out=None, stream=None):
         """q [B, T, nh, hd] and k [B, T, nkv, hd] (or None) rotated to positions [B, T]; written to
         q_out and k_out (new dense tensors unless given; q and k themselves are allowed)."""
+        if k is None and k_out is not None:
+            raise ValueError("k_out without k")
         if q_out is None:
             q_out = _new(q, q.dtype, stream)
         if k_out is None and k is not None:
@@ -630,6 +636,8 @@ class Rope:
     def qk_norm(self, q, k, v, positions, q_norm_w=None, k_norm_w=None, eps=1e-6, q_out=None,
                 k_out=None, v_out=None, stream=None):
         """RMS norms of q, k (weighted) and v (unweighted; None: absent), q and k rotated."""
+        if (k is None and k_out is not None) or (v is None and v_out is not None):
+            raise ValueError("k_out without k, or v_out without v")
         if q_out is None:
             q_out = _new(q, q.dtype, stream)
         if k_out is None and k is not None:
@@ -646,7 +654,7 @@ class Rope:
 class Kv4Cache:
     """A cache of K and V in 4 bits (a dg_attn_kv4): codes k, v [batch, nkv, cap, hd/2] and scales
     k_scale, v_scale [batch, nkv, cap, hd/16], all uint8.  `buffers`: these four, or None for new
-    ones filled with zeros."""
+    ones filled with zeros.  They are the cache's for its life: written into, not replaced."""
 
     def __init__(self, batch, nkv, cap, hd, buffers=None, device=None):
         torch = _torch()

@@ -107,3 +107,16 @@ def test_strides_beyond_the_address_space(lib):
         assert call(lib, rope, BASE, [768, 256, 64], BASE << 1, [s, 256, 64], [2, 3, 4]) == B.DG_ERR_ARG
     top = 2 ** 31 - 1
     assert lib.dg_attn_kv4_append(kv4(batch=top, nkv=top, cap=top), None, None) == B.DG_ERR_ARG
+
+
+def test_outputs_of_absent_tensors():
+    """An output for a tensor that is not there would come back as it was."""
+    q, pos = torch.zeros(2, 3, 4, 64, dtype=torch.float16), torch.zeros(2, 3, dtype=torch.int64)
+    build_mod.build()
+    rope = B.Rope(64)
+    with pytest.raises(ValueError, match="k_out without k"):
+        rope.apply(q, None, pos, k_out=q)
+    with pytest.raises(ValueError, match="k_out without k"):
+        rope.qk_norm(q, None, None, pos, k_out=q)
+    with pytest.raises(ValueError, match="v_out without v"):
+        rope.qk_norm(q, q, None, pos, v_out=q)
