@@ -97,7 +97,7 @@ __host__ __device__ inline Visible visible_keys(const WindowParams &p, int nq, i
 cudaError_t launch_window_rows(const WindowParams &p, int hd, cudaStream_t s);
 
 // Rows of a kv head (T * G) that launch_window_few takes: up to where the tile kernel is as fast.  us, few
-// against tiles, 8 sequences of 8192 keys, 4 kv heads (and one of 2048):
+// against tiles, 8 sequences of 8192 keys, 4 kv heads (and one of 2048), bf16 (f16: the same within 3):
 //   16-bit  hd 64:   8 rows 30 31 (13 13), 16 rows 34 30 (15 13)
 //           hd 128:  2 rows 42 47 (15 15), 8 rows 44 46 (17 15), 16 rows 50 47 (22 15)
 //           hd 256:  2 rows 67 66 (16 18), 8 rows 73 67 (22 17)

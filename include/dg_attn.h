@@ -392,7 +392,9 @@ int dg_attn_kv4_append(const dg_attn_kv4 *cache, const dg_attn_kv4_args *args, c
  * (right >= 0; -1: no limit), and j >= p - left (left >= 0; -1: no limit) or j < sinks, the first
  * tokens that stay visible.  out = sum_j softmax_j(scale q.k_j) v_j over the keys it sees; a row that
  * sees none, or only keys whose scores are -inf, is 0; rows i >= q_len[b] of out are left as they were.  What stands in rows that a query
- * does not see, NaN and infinities included, has no part in it.  kv head of q head h: h / (nh/nkv). */
+ * does not see, NaN and infinities included, has no part in it.  kv head of q head h: h / (nh/nkv).
+ * Scores, their sums and the sums of weighted rows are fp32; weights are rounded to the type of V (half a
+ * step, relative; f16 also to 2^-30 of the row's largest weight). */
 typedef struct dg_attn_window_plan dg_attn_window_plan;
 
 typedef struct dg_attn_window_args {
@@ -410,7 +412,7 @@ dg_attn_window_plan *dg_attn_window_plan_create(int nh, int nkv, int hd, int bat
 void dg_attn_window_plan_destroy(dg_attn_window_plan *plan);
 int dg_attn_window_attend(dg_attn_window_plan *plan, const dg_attn_window_args *args,
                           cudaStream_t stream);
-/* The same over a 4-bit cache; q and out in `type`, the products in f16 with fp32 sums. */
+/* The same over a 4-bit cache; q and out in `type`, the products in f16 with fp32 sums, weights in f16. */
 int dg_attn_window_attend_kv4(dg_attn_window_plan *plan, const dg_attn_window_args *args,
                               const dg_attn_kv4 *cache, cudaStream_t stream);
 /* Synchronise `stream`, then read and clear the plan's device status word: DG_OK, or
